@@ -55,25 +55,26 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // A 16x16 product over a 32-deep slice: lane l = 16 g + c supplies row (A) or column (B)
 // c at the contraction indices 8 g + e, e = 0..7, and receives D[4 g + i][c], i = 0..3.
 //
-// Parts.  A float32 value that meets a bf16 matrix-core operand is rounded to it, or
-// written as a sum of bf16 values, each the rounding of what the ones before left: two
-// parts keep 16 bits, three all 24.
-//  * The state and the scores, where they meet q and v, take one part: their result is
-//    rounded to bf16 at the end, and the rounding of either is what a change of q or v by
-//    half a bf16 step would do (two roundings in place of one: 1.4 times the error).
+// Parts.  A float32 value that meets a bf16 matrix-core operand is written as a sum of bf16
+// values, each the rounding of what the ones before left (by at most 2^-8): two parts leave
+// 2^-16 of the value, three 2^-24.
+//  * The state and the scores take two where they meet q and v.  A result that is rounded to
+//    bf16 then errs like the rounded exact one, and a float32 result keeps 16 bits of a term.
+//    With one part the outputs err by 0.0023 of their norm in place of 0.0017, float32 ones
+//    by as much (packed prefill 350 us in place of 405, gradients 246 in place of 264).
 //  * The decayed values, which build the float32 states, take three where they are a part
-//    of a state that is handed out, so that it is as exact as a float32 sum.  Two (2^-17 of
-//    each term) where the state only meets q, and for tokens so far from the sequence's end
-//    that their weight in the last state is below 2^-8: their error there is 2^-25.
-// Matrix-core products a 64-token chunk at K = V = 128: 600 and 472 of 16x16x32 (776 with
-// two parts of state and scores); at a border 384 and 256.
+//    of a state that is handed out, so that it is as exact as a float32 sum.  Two where the
+//    state only meets q, and for tokens so far from the sequence's end that their weight in
+//    the last state is below 2^-8: their error there is 2^-25.
+// Matrix-core products a 64-token chunk at K = V = 128: 776 and 648 of 16x16x32; at a border
+// 384 and 256.
 
 template <typename T> struct Op;
 
 template <> struct Op<uint16_t> {
   using elem = uint16_t;
   static constexpr int kChunk = 64;
-  static constexpr int kValueParts = 3;
+  static constexpr int kStateParts = 2, kScoreParts = 2, kValueParts = 3;
   using frag = bf16x8;
   static __device__ __forceinline__ f32x4 mma(const frag &a, const frag &b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -127,23 +128,22 @@ template <> struct Op<uint16_t> {
       }
     }
   }
-  static __device__ __forceinline__ frag round(const float (&x)[8]) {
-    frag f[1];
-    parts(x, f);
-    return f[0];
-  }
-  // four consecutive scores
-  static __device__ __forceinline__ void store4(elem *p, float (&x)[4]) {
-    const bf16x2 a = part(x[0], x[1], false), b = part(x[2], x[3], false);
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+  // four consecutive scores, a part to each matrix
+  static __device__ __forceinline__ void store4(elem *p, int stride, float (&x)[4]) {
+#pragma unroll
+    for (int n = 0; n < kScoreParts; ++n) {
+      const bool more = n + 1 < kScoreParts;
+      const bf16x2 a = part(x[0], x[1], more), b = part(x[2], x[3], more);
+      *reinterpret_cast<uint2 *>(p + n * stride) =
+          make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+    }
   }
 };
 
 template <> struct Op<float> {
   using elem = float;
   static constexpr int kChunk = 32;
-  static constexpr int kValueParts = 1;
+  static constexpr int kStateParts = 1, kScoreParts = 1, kValueParts = 1;
   struct frag { float v[8]; };
   static __device__ __forceinline__ f32x4 mma(const frag &a, const frag &b, f32x4 c) {
 #pragma unroll
@@ -174,12 +174,7 @@ template <> struct Op<float> {
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[0].v[e] = x[e];
   }
-  static __device__ __forceinline__ frag round(const float (&x)[8]) {
-    frag f[1];
-    parts(x, f);
-    return f[0];
-  }
-  static __device__ __forceinline__ void store4(elem *p, float (&x)[4]) {
+  static __device__ __forceinline__ void store4(elem *p, int, float (&x)[4]) {
     *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
   }
 };
@@ -258,7 +253,7 @@ template <typename T, int DQ, int DV, bool OUTPUT> struct Lds {
   T q[OUTPUT ? C * ldq : 8];   // the sums at the borders use neither q nor scores
   T k[C * ldk];
   T v[C * ldv];
-  alignas(16) T score[OUTPUT ? C * lds : 8];
+  alignas(16) T score[Op<T>::kScoreParts][OUTPUT ? C * lds : 8];
   float pw[C + 1];
   // s_intra times the weight of key 4 g + e behind token c, the tiles 16 * [i] tokens apart
   alignas(16) float gap[OUTPUT ? C / 16 : 1][64][4];
@@ -474,7 +469,7 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
     lds.upd[i] = i < C ? R.s_upd * lds.pw[max(C - i - off, 0)] : 0.0f;
   // score tiles above the diagonal stay zero
   if constexpr (OUTPUT)
-    for (int i = threadIdx.x; i < C * L::lds * static_cast<int>(sizeof(T)) / 16; i += NT)
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(lds.score)) / 16; i += NT)
       reinterpret_cast<u32x4 *>(lds.score)[i] = u32x4{0, 0, 0, 0};
 
   // heads and head of an operand: the value heads, or the q/k heads (div: of `group`)
@@ -620,7 +615,7 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
 #pragma unroll
           for (int e = 0; e < 4; ++e)   // masked, not weighted: a key behind may not be finite
             x[e] = ti[m] > tj[m] || c >= 4 * g + e ? d[m][e] * w[e] : 0.0f;
-          O::store4(lds.score + (16 * ti[m] + c) * L::lds + 16 * tj[m] + 4 * g, x);
+          O::store4(lds.score[0] + (16 * ti[m] + c) * L::lds + 16 * tj[m] + 4 * g, C * L::lds, x);
         }
       }
 
@@ -642,7 +637,7 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
           for (int it = 0; it < IT; ++it) acc[ct][it] = zero4();
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          typename O::frag sf[CT];
+          typename O::frag sf[CT][O::kStateParts];
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct) {
             float x[8];
@@ -651,7 +646,7 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
               x[e] = S[2 * s][ct][e];
               x[4 + e] = S[2 * s + 1][ct][e];
             }
-            sf[ct] = O::round(x);
+            O::parts(x, sf[ct]);
           }
           // products of one accumulator apart from each other, here and below: a dependent
           // one would wait out its predecessor's latency
@@ -659,7 +654,9 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
           for (int it = 0; it < IT; ++it) {
             const typename O::frag qf = O::rows(lds.q, L::ldq, 16 * it + c, 32 * s, g);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) acc[ct][it] = O::mma(sf[ct], qf, acc[ct][it]);
+            for (int n2 = 0; n2 < O::kStateParts; ++n2)
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) acc[ct][it] = O::mma(sf[ct][n2], qf, acc[ct][it]);
           }
         }
         __syncthreads();   // the scores of the other waves
@@ -671,12 +668,13 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
         }
 #pragma unroll
         for (int js = 0; js < JS; ++js)
+          for (int n2 = 0; n2 < O::kScoreParts; ++n2)
 #pragma unroll
-          for (int it = 2 * js; it < IT; ++it) {
-            const typename O::frag af = O::rows(lds.score, L::lds, 16 * it + c, 32 * js, g);
+            for (int it = 2 * js; it < IT; ++it) {
+              const typename O::frag af = O::rows(lds.score[n2], L::lds, 16 * it + c, 32 * js, g);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) acc[ct][it] = O::mma(vf[js][ct], af, acc[ct][it]);
-          }
+              for (int ct = 0; ct < CT; ++ct) acc[ct][it] = O::mma(vf[js][ct], af, acc[ct][it]);
+            }
       }
 
       if constexpr (OUTPUT) {

@@ -377,8 +377,8 @@ typedef struct {
  * structure or function before them.
  *
  * Arithmetic: float32 states, scores and sums for both input types.  With BF16 inputs the
- * state and the scores are rounded to bf16 where they meet q and v, and the terms of the
- * float32 states keep 24 bits; no value range narrower than bf16's applies.  A head's
+ * state and the scores keep 16 bits where they meet q and v (float32 outputs too), and the
+ * terms of the float32 states keep 24 bits; no value range narrower than bf16's applies.  A head's
  * weight lambda^n that is zero in float32 ends the reach of a token.  Inputs that are not
  * finite make the outputs of their own token and of later tokens of the sequence (in the
  * backward also of earlier ones) not finite; tokens out of their reach may be spared, and
