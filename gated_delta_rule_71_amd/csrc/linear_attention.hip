@@ -63,9 +63,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 //    With one part the outputs err by 0.0023 of their norm in place of 0.0017, float32 ones
 //    by as much (packed prefill 350 us in place of 405, gradients 246 in place of 264).
 //  * The decayed values, which build the float32 states, take three where they are a part
-//    of a state that is handed out, so that it is as exact as a float32 sum.  Two where the
-//    state only meets q, and for tokens so far from the sequence's end that their weight in
-//    the last state is below 2^-8: their error there is 2^-25.
+//    of a state that is handed out, so that it is as exact as a float32 sum: all tokens whose
+//    weight in it is not zero, as far ones can be all that it has (large at a prompt's start,
+//    zeros behind).  Two where the state only meets q.
 // Matrix-core products a 64-token chunk at K = V = 128: 776 and 648 of 16x16x32; at a border
 // 384 and 256.
 
@@ -193,11 +193,6 @@ __device__ __forceinline__ float decay_power(float g, int n) {
 // number.  What lies farther back adds nothing.
 __device__ __forceinline__ long decay_reach(float g) {
   return g < 0.0f ? static_cast<long>(fminf(ceilf(104.0f / -g), 1.0e9f)) : 1L << 40;
-}
-
-// Tokens after which a head's weight is below 2^-8.
-__device__ __forceinline__ long decay_near(float g) {
-  return g < 0.0f ? static_cast<long>(fminf(ceilf(5.5452f / -g), 1.0e9f)) : 1L << 40;
 }
 
 // Four lanes' four elements, transposed: lane 4 q + j gets element j of lanes 4 q .. 4 q + 3.
@@ -455,7 +450,7 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
     while (tj[m] > ti[m]) tj[m] -= ++ti[m];
   }
 
-  const long near = decay_near(gh);
+  const long reach = decay_reach(gh);
   const int off = R.reverse ? 0 : 1;
   if (threadIdx.x == 0) lds.mark = 0;
   for (int i = threadIdx.x; i <= C; i += NT) lds.pw[i] = decay_power(gh, i);
@@ -537,7 +532,6 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
     }
     if constexpr (!OUTPUT) {
       // only the tokens that the border is in reach of
-      const long reach = decay_reach(gh);
       if (R.reverse) b = min(b, a + reach);
       else a = max(a, b - reach);
     }
@@ -578,7 +572,7 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
       if (OUTPUT && bad) lds.mark = 1;
       __syncthreads();
       const long base = low, after = left - r;
-      const bool exact = R.exact_state && (R.reverse ? low - t0 : t1 - low - r) < near;
+      const bool exact = R.exact_state && (R.reverse ? low - t0 : t1 - low - r) < reach;
       next = static_cast<int>(min(static_cast<long>(C), after));
       if (after > 0) load_tiles(R.reverse ? low - next : low + r, next);
 

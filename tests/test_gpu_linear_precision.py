@@ -40,11 +40,13 @@ def normal(seed, *shape):
 
 
 def one_term(x, r, bound, what):
-    """Every element within ``bound`` of the reference's element; zeros are zeros."""
+    """Every element within ``bound`` of the reference's element; zeros are zeros.  Below 2^-126
+    float32 has the spacing of 2^-126 itself, 2^-149, so that a rounding there is by at most
+    2^-150 = 2^-126 u, and later weights are at most 1: the bound is taken of |r| + 2^-126."""
     x = to_host(x)
     assert x.shape == r.shape and np.all(np.isfinite(x)), what
     assert np.all(x[r == 0] == 0), what
-    off = np.max(np.abs(x - r)[r != 0] / np.abs(r)[r != 0])
+    off = np.max(np.abs(x - r) / (np.abs(r) + 2.0 ** -126))
     assert off <= bound, f"{what}: {off / U:.1f} u, bound {bound / U:.1f} u"
 
 
@@ -134,3 +136,79 @@ def test_gradients_of_random_inputs(Hk, Hv, K, V, lens):
                       initial_state=s0, cu_seqlens=cu)
     for name, x, r in zip(("dq", "dk", "dv"), got, ref):
         of_norm(x, rounded(r), 2.0 ** -10.5, name)
+
+
+def far_value(seed, T, H, D, at):
+    """Rows of which one has values (its head's value channels, or one q/k channel of 1)."""
+    x = np.zeros((1, T, H, D))
+    x[0, at] = W.as_f64(normal(seed, H, D))
+    return x
+
+
+@pytest.mark.parametrize("K,V", [(64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T,at", [(1, 0), (64, 2), (200, 3), (300, 100), (320, 1)])
+def test_state_of_far_tokens(K, V, T, at):
+    """k and v of one token alone, zeros behind it (a prompt padded at its end): the final
+    state is that token's term, however far its weight has fallen.  In batched rows, a packed
+    slot cache with other sequences around it, and for the gradient of the initial state."""
+    import torch
+    import gated_delta_rule_71_amd as gdr
+    H = 3
+    g = np.array([-0.002, -0.06, -0.25], np.float32)
+    k, v = far_value(21, T, H, K, at), far_value(22, T, H, V, at)
+    q = W.as_f64(normal(23, 1, T, H, K))
+    bound = (6 * -(-T // 64) + 14) * U
+    d = [to_dev(bf16(x)) for x in (q, k, v)]
+    _, fs = gdr.chunk_linear_attention(*d, to_dev(g), output_final_state=True)
+    _, r = LA.prefill(q, k, v, g)
+    one_term(fs, r, bound, "final state")
+
+    other = [to_dev(normal(s, 1, 70, H, n)) for s, n in ((24, K), (25, K), (26, V))]
+    packed = [torch.cat([y, x, y], 1) for x, y in zip(d, other)]
+    cu = torch.tensor([0, 70, 70 + T, 140 + T], dtype=torch.int32, device="cuda")
+    cache = torch.zeros((4, H, K, V), device="cuda")
+    slots = torch.tensor([3, 1, 0], dtype=torch.int32, device="cuda")
+    gdr.chunk_linear_attention(*packed, to_dev(g), initial_state=cache, cu_seqlens=cu,
+                               state_indices=slots)
+    one_term(cache[1:2], r, bound, "slot")
+
+    # back in time: q and do of one token alone, zeros before it
+    qf, do = k[:, ::-1], v[:, ::-1]
+    *_, dh0 = gdr.chunk_linear_attention_backward(
+        to_dev(bf16(qf)), d[0], to_dev(normal(27, 1, T, H, V)), to_dev(g), to_dev(bf16(do)))
+    *_, r = LA.backward(qf, q, np.zeros((1, T, H, V)), g, do)
+    one_term(dh0, r, bound, "dh0")
+
+
+@pytest.mark.parametrize("K,V", [(64, 128), (128, 128)])
+def test_states_padded_with_zeros(K, V):
+    """Random tokens, then zeros, as in rows that are filled up: float32 sums of at most two
+    chunks of terms (each within 26 u of itself), then carries of 5 u each."""
+    import gated_delta_rule_71_amd as gdr
+    T, real, H = 320, 120, 2
+    g = np.array([-0.01, -0.05], np.float32)
+    q, k, v = (W.as_f64(normal(s, 1, T, H, n)) for s, n in ((31, K), (32, K), (33, V)))
+    k[:, real:], v[:, real:] = 0, 0
+    _, fs = gdr.chunk_linear_attention(*(to_dev(bf16(x)) for x in (q, k, v)), to_dev(g),
+                                       output_final_state=True)
+    _, r = LA.prefill(q, k, v, g)
+    of_norm(fs, r, (26 + 6 * 5) * U / 3 ** 0.5, "final state")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 2])
+def test_state_of_a_decoded_token(dtype, T):
+    """lambda S + k v: expf (2 u), its product and the fused sum (u each), of T tokens."""
+    import gated_delta_rule_71_amd as gdr
+    n, H, K, V = 3, 2, 128, 64
+    r = np.random.default_rng(41)
+    q, k, v = (W.store(r.standard_normal((n, T, H, d), dtype=np.float32),
+                       W.BF16 if dtype == "bf16" else W.F32) for d in (K, K, V))
+    g = np.array([-0.3, -4.0], np.float32)
+    cache = r.standard_normal((n, H, K, V)).astype(np.float32)
+    d = to_dev(cache)
+    gdr.linear_attention_decode(*(to_dev(x if T > 1 else x[:, 0]) for x in (q, k, v)), to_dev(g), d)
+    f = [W.as_f64(x) for x in (q, k, v)]
+    _, after, _ = LA.decode(*f, g, cache, np.arange(n))
+    _, m, _ = LA.decode(*map(np.abs, f), g, np.abs(cache), np.arange(n))
+    assert np.all(np.abs(to_host(d) - after) <= 4 * T * U * m)
