@@ -766,6 +766,17 @@ namespace {
 // blocks of 256 threads whose grid stays within the launch limit of 2^32 threads
 constexpr int64_t kMaxBlocks = int64_t{1} << 24;
 
+// whether two arrays share memory (NULL: no array)
+bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + b_bytes && y < x + a_bytes;
+}
+
+template <typename Args>
+size_t states_bytes(const Args *a, int64_t states) {
+  return static_cast<size_t>(states) * a->num_v_heads * a->head_k * a->head_v * sizeof(float);
+}
+
 // the checks a linear-attention prefill and its backward share
 template <typename Args>
 int check_linear(const Args *a) {
@@ -861,13 +872,10 @@ int gdr_validate_linear_prefill(const gdr_linear_prefill_args *a) {
   if (st != GDR_OK) return st;
   if (a->state_indices && a->num_slots <= 0) return GDR_ERR_INVALID_ARG;
   if (a->final_state && !aligned16(a->final_state)) return GDR_ERR_INVALID_ARG;
-  if (a->initial_state && a->final_state && a->initial_state != a->final_state) {
-    const int64_t states = a->state_indices ? a->num_slots : a->num_seqs;
-    const uintptr_t bytes = states * a->num_v_heads * a->head_k * a->head_v * sizeof(float);
-    const uintptr_t i = reinterpret_cast<uintptr_t>(a->initial_state);
-    const uintptr_t f = reinterpret_cast<uintptr_t>(a->final_state);
-    if (i < f + bytes && f < i + bytes) return GDR_ERR_INVALID_ARG;
-  }
+  const size_t states = states_bytes(a, a->state_indices ? a->num_slots : a->num_seqs);
+  if (a->initial_state != a->final_state &&
+      overlap(a->initial_state, states, a->final_state, states))
+    return GDR_ERR_INVALID_ARG;
   if (int64_t{a->batch} * a->seqlen > 0) {
     if (!a->q || !a->k || !a->v || !a->out) return GDR_ERR_INVALID_ARG;
     if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out))
@@ -975,6 +983,11 @@ int gdr_validate_linear_backward(const gdr_linear_backward_args *a) {
   if (tokens * a->num_qk_heads * a->head_k >= (int64_t{1} << 34)) return GDR_ERR_UNSUPPORTED;
   if ((a->d_final_state && !aligned16(a->d_final_state)) ||
       (a->d_initial_state && !aligned16(a->d_initial_state)))
+    return GDR_ERR_INVALID_ARG;
+  // written by some workgroups while others of the same launch read the states
+  const size_t states = states_bytes(a, a->num_seqs);
+  if (overlap(a->d_initial_state, states, a->d_final_state, states) ||
+      overlap(a->d_initial_state, states, a->initial_state, states))
     return GDR_ERR_INVALID_ARG;
   if (tokens > 0) {
     for (const void *t : {a->q, a->k, a->v, a->d_out, static_cast<const void *>(a->dq),

@@ -451,7 +451,8 @@ typedef struct {
  * over the value heads that read it.  Rows of dq, dk, dv behind the last sequence are not
  * written.
  * Workspace: gdr_linear_backward_workspace_bytes, 256-byte aligned, contents irrelevant.
- * Supported as the prefill, and Tt * Hk * K < 2^34.  Outputs alias nothing.
+ * Supported as the prefill, and Tt * Hk * K < 2^34.  Outputs alias nothing; a
+ * d_initial_state that overlaps d_final_state or initial_state is refused.
  */
 typedef struct {
   int32_t batch;

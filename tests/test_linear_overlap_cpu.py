@@ -1,0 +1,61 @@
+"""Arrays that may not overlap: the linear attention's and group norm's C entry points refuse
+them before anything is enqueued (no GPU calls; addresses are never dereferenced)."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import pytest
+
+from gated_delta_rule_71_amd import _lib
+
+OK, INVALID = 0, 1
+MB = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def at(n):
+    """Device addresses 64 MB apart, the first of them 64 MB."""
+    return (n + 1) * 64 * MB
+
+
+def args(struct, base, kw):
+    a = struct()
+    for k, v in {**base, **kw}.items():
+        setattr(a, k, v)
+    return a
+
+
+def backward(**kw):
+    """2 rows of 100 tokens, 4 heads of 128 x 64, bf16; states of 256 KB."""
+    return args(_lib.LinearBackwardArgs, dict(
+        batch=2, seqlen=100, num_seqs=2, num_qk_heads=4, num_v_heads=4, head_k=128, head_v=64,
+        qkv_dtype=1, scale=math.nan, q=at(0), k=at(1), v=at(2), g=at(3), d_out=at(4), dq=at(5),
+        dk=at(6), dv=at(7), initial_state=at(8), d_final_state=at(9), d_initial_state=at(10)), kw)
+
+
+STATES = 4 * 2 * 4 * 128 * 64
+
+
+@pytest.mark.parametrize("kw", [
+    dict(d_initial_state=at(9)), dict(d_initial_state=at(8)),
+    dict(d_initial_state=at(9) + STATES - 16), dict(d_initial_state=at(8) - STATES + 16),
+    dict(d_initial_state=at(9), initial_state=0), dict(d_initial_state=at(8), d_final_state=0),
+    dict(d_initial_state=at(9), seqlen=0)], ids=str)
+def test_backward_states(lib, kw):
+    """The gradient of the initial states is written while other workgroups read the states."""
+    a = backward(**kw)
+    assert lib.gdr_validate_linear_backward(ctypes.byref(a)) == INVALID
+    assert lib.gdr_chunk_linear_attention_backward(ctypes.byref(a), None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    {}, dict(d_initial_state=at(9) + STATES), dict(d_initial_state=at(8) - STATES),
+    dict(d_initial_state=0), dict(d_final_state=0, initial_state=0),
+    dict(initial_state=at(9)), dict(d_initial_state=at(9), batch=0, num_seqs=0)], ids=str)
+def test_backward_states_apart(lib, kw):
+    assert lib.gdr_validate_linear_backward(ctypes.byref(backward(**kw))) == OK
