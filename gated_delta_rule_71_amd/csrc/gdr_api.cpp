@@ -955,6 +955,10 @@ int gdr_linear_attention_decode(const gdr_linear_decode_args *a, void *stream) {
   const int st = gdr_validate_linear_decode(a);
   if (st != GDR_OK) return st;
   if (a->batch == 0) return GDR_OK;
+  // a state between tokens would land in a slot that another workgroup reads
+  if (overlap(a->intermediate_state, states_bytes(a, int64_t{a->batch} * a->num_tokens), a->state,
+              states_bytes(a, a->num_slots)))
+    return GDR_ERR_INVALID_ARG;
   gdr::LinearDecodeParams p{};
   p.q = a->q;
   p.k = a->k;

@@ -421,7 +421,8 @@ typedef struct {
 /*
  * Decode over a slot-indexed float32 state cache, in place: one or several tokens per
  * request, as gdr_decode_args.  q, k [n, T, Hk, K]; v, out [n, T, Hv, V]; g [Hv].
- * Supported: K, V in {64, 128}, 1 <= T <= 2^16, n * Hv < 2^24.  `out` aliases no input.
+ * Supported: K, V in {64, 128}, 1 <= T <= 2^16, n * Hv < 2^24.  `out` aliases no input;
+ * an intermediate_state that overlaps the state is refused by the enqueue call.
  */
 typedef struct {
   int32_t batch;            /* n requests                                           */

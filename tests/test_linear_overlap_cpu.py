@@ -59,3 +59,32 @@ def test_backward_states(lib, kw):
     dict(initial_state=at(9)), dict(d_initial_state=at(9), batch=0, num_seqs=0)], ids=str)
 def test_backward_states_apart(lib, kw):
     assert lib.gdr_validate_linear_backward(ctypes.byref(backward(**kw))) == OK
+
+
+def decode(**kw):
+    """8 requests of 3 tokens, 4 heads of 128 x 64, bf16; 16 slots of 128 KB."""
+    return args(_lib.LinearDecodeArgs, dict(
+        batch=8, num_tokens=3, num_qk_heads=2, num_v_heads=4, head_k=128, head_v=64, num_slots=16,
+        qkv_dtype=1, out_dtype=1, scale=math.nan, q=at(0), k=at(1), v=at(2), g=at(3), state=at(4),
+        intermediate_state=at(5), out=at(6)), kw)
+
+
+SLOT = 4 * 4 * 128 * 64
+
+
+@pytest.mark.parametrize("kw", [
+    dict(intermediate_state=at(4)), dict(intermediate_state=at(4) + 16 * SLOT - 16),
+    dict(intermediate_state=at(4) - 8 * 3 * SLOT + 16),
+    dict(intermediate_state=at(4) + SLOT, num_tokens=1)], ids=str)
+def test_decode_states_between(lib, kw):
+    """The states between the tokens would overwrite slots that other workgroups read."""
+    assert lib.gdr_linear_attention_decode(ctypes.byref(decode(**kw)), None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(intermediate_state=at(4) + 16 * SLOT),
+                                dict(intermediate_state=at(4) - 8 * 3 * SLOT)], ids=str)
+def test_decode_states_apart(lib, kw):
+    a = decode(**kw)
+    assert lib.gdr_validate_linear_decode(ctypes.byref(a)) == OK
+    a.batch = 0
+    assert lib.gdr_linear_attention_decode(ctypes.byref(a), None) == OK
