@@ -4,6 +4,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include <hip/hip_runtime.h>
@@ -766,11 +767,29 @@ namespace {
 // blocks of 256 threads whose grid stays within the launch limit of 2^32 threads
 constexpr int64_t kMaxBlocks = int64_t{1} << 24;
 
-// whether two arrays share memory (NULL: no array)
+// whether two arrays share memory (NULL or no bytes: no array)
 bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + b_bytes && y < x + a_bytes;
+  return a && b && a_bytes && b_bytes && x < y + b_bytes && y < x + a_bytes;
 }
+
+struct Range {
+  const void *p;
+  size_t bytes;
+};
+
+// no array that is written shares memory with another one
+bool apart(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+  for (const Range &w : written) {
+    for (const Range &r : read)
+      if (overlap(w.p, w.bytes, r.p, r.bytes)) return false;
+    for (const Range &o : written)
+      if (&o != &w && overlap(w.p, w.bytes, o.p, o.bytes)) return false;
+  }
+  return true;
+}
+
+size_t dtype_bytes(int32_t dtype) { return dtype == GDR_DTYPE_F32 ? 4 : 2; }
 
 template <typename Args>
 size_t states_bytes(const Args *a, int64_t states) {
@@ -894,6 +913,17 @@ int gdr_chunk_linear_attention(const gdr_linear_prefill_args *a, void *stream) {
   if (st != GDR_OK) return st;
   if (a->num_seqs == 0) return GDR_OK;
   const LinearLayout l = linear_layout(a, false);
+  const size_t tokens = static_cast<size_t>(a->batch) * a->seqlen, e = dtype_bytes(a->qkv_dtype);
+  const size_t keys = tokens * a->num_qk_heads * a->head_k;
+  const size_t values = tokens * a->num_v_heads * a->head_v;
+  const size_t states = states_bytes(a, a->state_indices ? a->num_slots : a->num_seqs);
+  const float *initial = a->initial_state == a->final_state ? nullptr : a->initial_state;
+  if (!apart({{a->out, values * dtype_bytes(a->out_dtype)}, {a->final_state, states},
+              {a->workspace, l.total}},
+             {{a->q, keys * e}, {a->k, keys * e}, {a->v, values * e}, {initial, states},
+              {a->g, 4u * a->num_v_heads}, {a->cu_seqlens, 4u * (a->num_seqs + size_t{1})},
+              {a->state_indices, 4u * size_t(a->num_seqs)}}))
+    return GDR_ERR_INVALID_ARG;
   char *ws = static_cast<char *>(a->workspace);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int f32 = a->qkv_dtype == GDR_DTYPE_F32;
@@ -955,9 +985,14 @@ int gdr_linear_attention_decode(const gdr_linear_decode_args *a, void *stream) {
   const int st = gdr_validate_linear_decode(a);
   if (st != GDR_OK) return st;
   if (a->batch == 0) return GDR_OK;
-  // a state between tokens would land in a slot that another workgroup reads
-  if (overlap(a->intermediate_state, states_bytes(a, int64_t{a->batch} * a->num_tokens), a->state,
-              states_bytes(a, a->num_slots)))
+  // (a state between tokens, say, would land in a slot that another workgroup reads)
+  const int64_t tokens = int64_t{a->batch} * a->num_tokens;
+  const size_t keys = tokens * a->num_qk_heads * a->head_k * dtype_bytes(a->qkv_dtype);
+  const size_t values = tokens * a->num_v_heads * a->head_v;
+  if (!apart({{a->out, values * dtype_bytes(a->out_dtype)}, {a->state, states_bytes(a, a->num_slots)},
+              {a->intermediate_state, states_bytes(a, tokens)}},
+             {{a->q, keys}, {a->k, keys}, {a->v, values * dtype_bytes(a->qkv_dtype)},
+              {a->g, 4u * a->num_v_heads}, {a->batch_indices, 4u * size_t(a->batch)}}))
     return GDR_ERR_INVALID_ARG;
   gdr::LinearDecodeParams p{};
   p.q = a->q;
@@ -1017,6 +1052,16 @@ int gdr_chunk_linear_attention_backward(const gdr_linear_backward_args *a, void 
   const int f32 = a->qkv_dtype == GDR_DTYPE_F32;
   const float scale = scale_or_default(a->scale, a->head_k);
   const LinearLayout l = linear_layout(a, true);
+  const size_t tokens = static_cast<size_t>(a->batch) * a->seqlen, e = dtype_bytes(a->qkv_dtype);
+  const size_t keys = tokens * a->num_qk_heads * a->head_k * e;
+  const size_t values = tokens * a->num_v_heads * a->head_v * e;
+  const size_t states = states_bytes(a, a->num_seqs);
+  if (!apart({{a->dq, keys}, {a->dk, keys}, {a->dv, values}, {a->d_initial_state, states},
+              {a->workspace, l.total}},
+             {{a->q, keys}, {a->k, keys}, {a->v, values}, {a->d_out, values},
+              {a->initial_state, states}, {a->d_final_state, states}, {a->g, 4u * a->num_v_heads},
+              {a->cu_seqlens, 4u * (a->num_seqs + size_t{1})}}))
+    return GDR_ERR_INVALID_ARG;
   char *ws = static_cast<char *>(a->workspace);
   const int K = a->head_k, V = a->head_v;
   gdr::LinearParams p = linear_params(a, true);

@@ -387,8 +387,8 @@ typedef struct {
  * Prefill: q [Tt, Hk, K], k [Tt, Hk, K], v [Tt, Hv, V], out [Tt, Hv, V]; g [Hv] float32.
  *   Rows of `out` behind the last sequence are not written.
  * Supported: K, V in {64, 128}; q/k/v F32 or BF16; out F32 or BF16;
- *   Tt < 2^31 - 1024, Hv <= 65536 and num_seqs * Hv < 2^22.  `out` aliases no input, and
- *   the two state arrays are one or do not overlap.
+ *   Tt < 2^31 - 1024, Hv <= 65536 and num_seqs * Hv < 2^22.  The arrays do not overlap,
+ *   but the two state arrays may be one.
  * Workspace: gdr_linear_prefill_workspace_bytes, 256-byte aligned, contents irrelevant: 0
  *   where one workgroup per sequence and head fills the chip or the tokens are few, else
  *   states at the borders of token windows.
@@ -421,8 +421,7 @@ typedef struct {
 /*
  * Decode over a slot-indexed float32 state cache, in place: one or several tokens per
  * request, as gdr_decode_args.  q, k [n, T, Hk, K]; v, out [n, T, Hv, V]; g [Hv].
- * Supported: K, V in {64, 128}, 1 <= T <= 2^16, n * Hv < 2^24.  `out` aliases no input;
- * an intermediate_state that overlaps the state is refused by the enqueue call.
+ * Supported: K, V in {64, 128}, 1 <= T <= 2^16, n * Hv < 2^24.  The arrays do not overlap.
  */
 typedef struct {
   int32_t batch;            /* n requests                                           */
@@ -606,7 +605,9 @@ int gdr_validate_backward(const gdr_backward_args *args);
 size_t gdr_backward_workspace_bytes(const gdr_backward_args *args);
 int gdr_chunk_gated_delta_rule_backward(const gdr_backward_args *args, void *stream);
 
-/* Linear attention: host-only checks, workspace sizes and enqueue. */
+/* Linear attention: host-only checks, workspace sizes and enqueue.  The enqueue calls also
+ * refuse (GDR_ERR_INVALID_ARG) an array that they would write and that overlaps another one,
+ * the workspace among them; only the prefill's final_state may be its initial_state. */
 int gdr_validate_linear_prefill(const gdr_linear_prefill_args *args);
 size_t gdr_linear_prefill_workspace_bytes(const gdr_linear_prefill_args *args);
 int gdr_chunk_linear_attention(const gdr_linear_prefill_args *args, void *stream);

@@ -88,3 +88,56 @@ def test_decode_states_apart(lib, kw):
     assert lib.gdr_validate_linear_decode(ctypes.byref(a)) == OK
     a.batch = 0
     assert lib.gdr_linear_attention_decode(ctypes.byref(a), None) == OK
+
+
+def prefill(**kw):
+    """2 rows of 400 tokens, 2/4 heads of 128 x 64, bf16: windows, and so a workspace."""
+    a = args(_lib.LinearPrefillArgs, dict(
+        batch=2, seqlen=400, num_seqs=2, num_qk_heads=2, num_v_heads=4, head_k=128, head_v=64,
+        qkv_dtype=1, out_dtype=1, scale=math.nan, q=at(0), k=at(1), v=at(2), g=at(3), out=at(4),
+        initial_state=at(5), final_state=at(6), workspace=at(7), workspace_bytes=32 * MB), kw)
+    return a
+
+
+ROWS = 2 * 400 * 2   # bytes of a bf16 channel of all tokens
+QK, V = ROWS * 2 * 128, ROWS * 4 * 64
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=at(0) + QK - 16), dict(out=at(1) - V + 16), dict(out=at(2) + 512),
+    dict(out=at(2) - 512), dict(out=at(2) - V, out_dtype=0), dict(out=at(3)),
+    dict(out=at(5) + STATES - 16), dict(out=at(6)), dict(out=at(7) + 4096), dict(final_state=at(1)),
+    dict(final_state=at(4) + 1024), dict(workspace=at(5)), dict(workspace=at(2) - 256)], ids=str)
+def test_prefill_outputs(lib, kw):
+    """Outputs (the workspace among them) that reach into an input or each other."""
+    assert lib.gdr_chunk_linear_attention(ctypes.byref(prefill(**kw)), None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=at(0) - 16), dict(out=at(1) + QK - 16), dict(out=at(2) + V - 64), dict(out=at(4) + SLOT),
+    dict(out=at(4) + 16 * SLOT - 16), dict(out=at(5) + 16), dict(intermediate_state=at(0)),
+    dict(intermediate_state=at(6) - 16 * SLOT), dict(state=at(1) - SLOT), dict(out=at(3))], ids=str)
+def test_decode_outputs(lib, kw):
+    kw = {**kw, "batch": 8, "num_tokens": 400 * 2 // 8}   # as many tokens as the prompts'
+    assert lib.gdr_linear_attention_decode(ctypes.byref(decode(**kw)), None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dq=at(0) + 16), dict(dk=at(1) - 16), dict(dv=at(4) + 256), dict(dq=at(6) + 16),
+    dict(dk=at(7) - 16), dict(dv=at(5) + 2 * 100 * 4 * 128 * 2 - 16), dict(dv=at(8)),
+    dict(dk=at(9) + 32), dict(d_initial_state=at(2)), dict(d_initial_state=at(5)),
+    dict(dq=at(3)), dict(num_qk_heads=2, workspace=at(4), workspace_bytes=32 * MB)], ids=str)
+def test_backward_outputs(lib, kw):
+    assert lib.gdr_chunk_linear_attention_backward(ctypes.byref(backward(**kw)), None) == INVALID
+
+
+def test_outputs_apart(lib):
+    """Arrays that touch, a state written in place, and arrays that are not given: past the
+    checks (an empty batch, so that nothing is enqueued)."""
+    for kw in ({}, dict(out=at(0) + QK), dict(out=at(2) - V), dict(final_state=at(5)),
+               dict(final_state=0, initial_state=0), dict(out=at(5) + STATES)):
+        assert lib.gdr_validate_linear_prefill(ctypes.byref(prefill(**kw))) == OK
+    none = dict(batch=0, num_seqs=0)
+    same = dict(out=at(0), final_state=at(0), initial_state=at(0))
+    assert lib.gdr_chunk_linear_attention(ctypes.byref(prefill(**none, **same)), None) == OK
+    assert lib.gdr_chunk_linear_attention_backward(ctypes.byref(backward(**none, dv=at(0))), None) == OK
