@@ -1175,6 +1175,17 @@ int check_group_norm(const Args *a) {
 }
 
 template <typename Args>
+size_t row_bytes(const Args *a) {
+  return static_cast<size_t>(a->tokens) * a->heads * a->group * dtype_bytes(a->dtype);
+}
+
+// rows that are read: none to look at where the output's rows are the same (each is read
+// by the lanes that write it, before they do)
+Range unless(const void *in, size_t rows, const void *out) {
+  return {in == out ? nullptr : in, rows};
+}
+
+template <typename Args>
 gdr::GroupNormParams group_norm_params(const Args *a) {
   gdr::GroupNormParams p{};
   p.x = a->x;
@@ -1205,6 +1216,10 @@ int gdr_validate_group_norm(const gdr_group_norm_args *a) {
 int gdr_group_norm(const gdr_group_norm_args *a, void *stream) {
   const int st = gdr_validate_group_norm(a);
   if (st != GDR_OK) return st;
+  const size_t rows = row_bytes(a), channels = 4u * size_t(a->heads) * a->group;
+  if (!apart({{a->out, rows}}, {unless(a->x, rows, a->out), unless(a->z, rows, a->out),
+                                {a->weight, channels}, {a->bias, channels}}))
+    return GDR_ERR_INVALID_ARG;
   gdr::GroupNormParams p = group_norm_params(a);
   p.out = a->out;
   const hipError_t e = gdr::launch_group_norm(p, a->dtype == GDR_DTYPE_F32,
@@ -1237,6 +1252,18 @@ int gdr_validate_group_norm_backward(const gdr_group_norm_backward_args *a) {
 int gdr_group_norm_backward(const gdr_group_norm_backward_args *a, void *stream) {
   const int st = gdr_validate_group_norm_backward(a);
   if (st != GDR_OK) return st;
+  const size_t rows = row_bytes(a), channels = 4u * size_t(a->heads) * a->group;
+  const size_t need = gdr_group_norm_backward_workspace_bytes(a);
+  void *const dz = a->z ? a->dz : nullptr;
+  const Range sums[3] = {{a->dweight, channels}, {a->dbias, channels}, {a->workspace, need}};
+  for (const void *out : {static_cast<const void *>(a->dx), static_cast<const void *>(dz)})
+    if (!apart({{out, rows}}, {unless(a->x, rows, out), unless(a->z, rows, out),
+                               unless(a->dy, rows, out), {a->weight, channels}, {a->bias, channels}}))
+      return GDR_ERR_INVALID_ARG;
+  if (!apart({{a->dx, rows}, {dz, rows}, sums[0], sums[1], sums[2]}, {}) ||
+      !apart({sums[0], sums[1], sums[2]}, {{a->x, rows}, {a->z, rows}, {a->dy, rows},
+                                           {a->weight, channels}, {a->bias, channels}}))
+    return GDR_ERR_INVALID_ARG;
   gdr::GroupNormParams p = group_norm_params(a);
   p.out = a->dx;
   p.dy = a->dy;

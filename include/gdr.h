@@ -489,7 +489,8 @@ typedef struct {
  * x, z, out [tokens, heads, group] (one dtype, F32 or BF16); weight, bias float32
  * [heads * group].  Supported: group a multiple of 8 up to 1024; heads <= 65536;
  * tokens * heads <= 2^26 - 1024.
- * out may be x or z itself.
+ * out may be x or z itself; apart from that no array that is written overlaps another one
+ * (refused by the enqueue call).
  */
 typedef struct {
   int32_t tokens;
@@ -508,7 +509,9 @@ typedef struct {
 /*
  * Its gradients: from dy = dL/dy (x's dtype) dx and, with a gate, dz (x's dtype), dweight
  * and dbias (float32 [heads * group], sums over the tokens in a fixed order; dbias may be
- * NULL).  Nothing of the forward call is needed.  dx may be dy itself.
+ * NULL).  Nothing of the forward call is needed.  dx and dz may each be x, z or dy
+ * itself; apart from that no array that is written overlaps another one (refused by the
+ * enqueue call).
  * Workspace: gdr_group_norm_backward_workspace_bytes, 16-byte aligned, contents irrelevant.
  */
 typedef struct {

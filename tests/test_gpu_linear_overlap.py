@@ -29,3 +29,33 @@ def test_python_outputs():
     final = buf[:2 * 64 * 64].view(1, 2, 64, 64)
     gdr.chunk_linear_attention(none, none, none, g, initial_state=state[:1], final_state=final)
     assert torch.equal(final, state[:1])
+
+
+@pytest.mark.parametrize("heads,group", [(5, 96), (3, 640)])
+def test_norm_rows_in_place(heads, group):
+    """Outputs over the rows that they are made from, and a view shifted by one row refused."""
+    import ctypes
+    import torch
+    import gated_delta_rule_71_amd as gdr
+    from gated_delta_rule_71_amd import _lib
+    lib = gdr.library()
+    x, z, dy = torch.randn((3, 301, heads, group), device="cuda", dtype=torch.bfloat16)
+    w, b = torch.randn((2, heads * group), device="cuda")
+    want = gdr.group_norm_backward(x, w, dy, b, z=z)
+    for over_dx, over_dz in (("dy", "z"), ("x", "dy"), ("z", "x")):
+        t = dict(x=x.clone(), z=z.clone(), dy=dy.clone())
+        dw, db = torch.empty_like(w), torch.empty_like(b)
+        a = _lib.GroupNormBackwardArgs(301, heads, group, _lib.GDR_DTYPE_BF16, 1, 1e-5,
+                                       t["x"].data_ptr(), t["z"].data_ptr(), w.data_ptr(),
+                                       b.data_ptr(), t["dy"].data_ptr(), t[over_dx].data_ptr(),
+                                       t[over_dz].data_ptr(), dw.data_ptr(), db.data_ptr())
+        ws = torch.empty(lib.gdr_group_norm_backward_workspace_bytes(ctypes.byref(a)),
+                         dtype=torch.uint8, device="cuda")
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+        assert lib.gdr_group_norm_backward(
+            ctypes.byref(a), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+        for got, r in zip((t[over_dx], dw, db, t[over_dz]), want):
+            assert torch.equal(got, r)
+    buf = torch.randn((302, heads, group), device="cuda")
+    with pytest.raises(RuntimeError):
+        gdr.group_norm(buf[:-1], w, b, out=buf[1:])

@@ -141,3 +141,37 @@ def test_outputs_apart(lib):
     same = dict(out=at(0), final_state=at(0), initial_state=at(0))
     assert lib.gdr_chunk_linear_attention(ctypes.byref(prefill(**none, **same)), None) == OK
     assert lib.gdr_chunk_linear_attention_backward(ctypes.byref(backward(**none, dv=at(0))), None) == OK
+
+
+def norm(**kw):
+    """40 tokens of 3 x 64 channels, bf16."""
+    return args(_lib.GroupNormArgs, dict(
+        tokens=40, heads=3, group=64, dtype=1, activation=1, eps=1e-5, x=at(0), z=at(1),
+        weight=at(2), bias=at(3), out=at(4)), kw)
+
+
+def norm_backward(**kw):
+    return args(_lib.GroupNormBackwardArgs, dict(
+        tokens=40, heads=3, group=64, dtype=1, activation=1, eps=1e-5, x=at(0), z=at(1),
+        weight=at(2), bias=at(3), dy=at(4), dx=at(5), dz=at(6), dweight=at(7), dbias=at(8),
+        workspace=at(9), workspace_bytes=MB), kw)
+
+
+NORM = 40 * 3 * 64 * 2
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=at(0) + 16), dict(out=at(0) - NORM + 16), dict(out=at(1) + NORM - 16),
+    dict(out=at(2) + 4 * 192 - 16), dict(out=at(3)), dict(out=at(0) + NORM - 16, z=0)], ids=str)
+def test_norm_output(lib, kw):
+    """Rows shifted against the ones that are read (the same rows are worked in place)."""
+    assert lib.gdr_group_norm(ctypes.byref(norm(**kw)), None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dx=at(0) + 16), dict(dx=at(4) - 16), dict(dx=at(1) + NORM - 16), dict(dz=at(5) + 16),
+    dict(dz=at(0) + 384), dict(dweight=at(0)), dict(dweight=at(5) + 32), dict(dbias=at(7) + 16),
+    dict(dbias=at(6)), dict(dx=at(2)), dict(workspace=at(4)), dict(workspace=at(5) + 1024),
+    dict(workspace=at(7) - 4096)], ids=str)
+def test_norm_gradients(lib, kw):
+    assert lib.gdr_group_norm_backward(ctypes.byref(norm_backward(**kw)), None) == INVALID
