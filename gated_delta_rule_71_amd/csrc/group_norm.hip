@@ -17,14 +17,31 @@ namespace gdr {
 
 namespace {
 
-// 1 / (1 + e^-x) on the hardware base-2 exponential and reciprocal (about an ulp each)
-__device__ __forceinline__ float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * 1.4426950408889634f));
+// p = 1 / (1 + e^-x) and q = 1 - p.  For bf16 rows on the hardware base-2 exponential and
+// reciprocal: the argument's rounding makes that |x| 2^-24 of p, far below a bf16 step.  For
+// float32 rows from e^-|x|, which cannot overflow, and q by itself, as 1 - p would lose it;
+// both within 6 2^-24 of themselves for every x.
+template <typename T> struct Sigmoid {
+  float p, q;
+  __device__ __forceinline__ Sigmoid(float x) {
+    p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * 1.4426950408889634f));
+    q = 1.0f - p;
+  }
+};
+template <> struct Sigmoid<float> {
+  float p, q;
+  __device__ __forceinline__ Sigmoid(float x) {
+    const float e = expf(-fabsf(x)), near = 1.0f / (1.0f + e), far = e * near;
+    p = x < 0.0f ? far : near;
+    q = x < 0.0f ? near : far;
+  }
+};
+template <typename T> __device__ __forceinline__ float act(float x, int kind) {
+  return kind ? x * Sigmoid<T>(x).p : x;
 }
-__device__ __forceinline__ float act(float x, int kind) { return kind ? x * sigmoid(x) : x; }
-__device__ __forceinline__ float act_slope(float x, int kind) {
-  const float p = sigmoid(x);
-  return kind ? p * (1.0f + x * (1.0f - p)) : 1.0f;
+template <typename T> __device__ __forceinline__ float act_slope(float x, int kind) {
+  const Sigmoid<T> s(x);
+  return kind ? s.p * (1.0f + x * s.q) : 1.0f;
 }
 
 __device__ __forceinline__ void put8(uint16_t *p, const float (&y)[8]) {
@@ -110,7 +127,7 @@ __global__ void __launch_bounds__(256) group_norm_kernel(const GroupNormParams p
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float n = p.bias ? fmaf(x[m][e], w[e], b[e]) : x[m][e] * w[e];
-      y[e] = GATE ? n * act(z[m][e], p.activation) : act(n, p.activation);
+      y[e] = GATE ? n * act<T>(z[m][e], p.activation) : act<T>(n, p.activation);
     }
     put8(static_cast<T *>(p.out) + at + m * STEP, y);
   }
@@ -184,10 +201,10 @@ __global__ void __launch_bounds__(256) group_norm_backward_kernel(const GroupNor
         const float n = fmaf(x[m][e], w[m][e], b[m][e]);
         float a;
         if constexpr (GATE) {
-          a = dy[m][e] * act(z[m][e], p.activation);
-          dz[e] = dy[m][e] * n * act_slope(z[m][e], p.activation);
+          a = dy[m][e] * act<T>(z[m][e], p.activation);
+          dz[e] = dy[m][e] * n * act_slope<T>(z[m][e], p.activation);
         } else {
-          a = dy[m][e] * act_slope(n, p.activation);
+          a = dy[m][e] * act_slope<T>(n, p.activation);
         }
         dw[m][e] += a * x[m][e];
         db[m][e] += a;

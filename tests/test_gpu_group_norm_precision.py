@@ -1,0 +1,58 @@
+"""GPU group norm in float32: the relative error of the gate and its slope over their whole range
+(marked gpu).
+
+Rows of +1 and -1 have the mean 0 and the deviation 1 exactly, so that with u = 2^-24 the
+normalised value is within 5 u (the mean square and eps u each, halved by the root; root,
+quotient and two products u each).  With e = exp(-|z|) (2 u), 1 / (1 + e) and e / (1 + e) are
+within 3 and 6 u.
+  * y = n z p:              5 + 6 + 2 products: 13 u, bound 14 u;
+  * dz = dy n p (1 + z q), p = 1 / (1 + exp(-z)) and q = 1 - p.  For z >= 0: p 3 u, z q (at most
+    0.28) 7 u of itself, so that the sum is within 2.6 u.  For z <= -3: p 6 u, z q 4 u of
+    itself, at most 1.6 times the sum: 7.4 u.  With n 5 u and three products: 17 and 22 u at
+    most, bound 22 u.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import group_norm as GN
+from parity import to_dev, to_host
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("lo,hi", [(-80.0, -3.0), (0.0, 80.0)])
+def test_gate_in_float32(lo, hi):
+    import gated_delta_rule_71_amd as gdr
+    r = np.random.default_rng(3)
+    shape = (40, 4, 128)
+    x = np.where(np.arange(128) % 2, 1.0, -1.0).astype(np.float32) * np.ones(shape, np.float32)
+    w = r.uniform(0.5, 2.0, 512).astype(np.float32)
+    z = np.linspace(lo, hi, x.size).astype(np.float32).reshape(shape)
+    dy = r.uniform(0.5, 2.0, shape).astype(np.float32)
+    y = gdr.group_norm(to_dev(x), to_dev(w), z=to_dev(z))
+    dz = gdr.group_norm_backward(to_dev(x), to_dev(w), to_dev(dy), z=to_dev(z))[3]
+    f = [a.astype(np.float64) for a in (x, w, dy, z)]
+    want = GN.group_norm(f[0], f[1], z=f[3])
+    grad = GN.group_norm_backward(*f[:3], z=f[3])[3]
+    for name, got, ref, bound in (("y", y, want, 14), ("dz", dz, grad, 22)):
+        off = np.max(np.abs(to_host(got) - ref) / np.maximum(np.abs(ref), 1e-37))
+        assert off <= bound * U, f"{name}: {off / U:.1f} u, bound {bound} u"
+
+
+def test_infinite_gates():
+    """exp(-|z|) neither overflows nor makes 0 times infinity: the limits of p and its slope."""
+    import torch
+    import gated_delta_rule_71_amd as gdr
+    x = torch.randn((1, 1, 8), device="cuda")
+    w = torch.ones(8, device="cuda")
+    z = torch.tensor([-3e38, -1000.0, -89.0, -0.0, 0.0, 89.0, 1000.0, 3e38], device="cuda")
+    for t in (torch.float32, torch.bfloat16):
+        n = gdr.group_norm(x.to(t), w, activation=None).double().flatten()
+        dy = torch.ones_like(x).to(t)
+        dz = gdr.group_norm_backward(x.to(t), w, dy, z=z.to(t).view(1, 1, 8))[3]
+        slope = torch.tensor([0, 0, 0, 0.5, 0.5, 1, 1, 1], device="cuda", dtype=torch.float64)
+        assert torch.all((dz.double().flatten() - n * slope).abs() <= 2.0 ** -6 * n.abs() + 1e-30)
