@@ -56,3 +56,19 @@ def test_infinite_gates():
         dz = gdr.group_norm_backward(x.to(t), w, dy, z=z.to(t).view(1, 1, 8))[3]
         slope = torch.tensor([0, 0, 0, 0.5, 0.5, 1, 1, 1], device="cuda", dtype=torch.float64)
         assert torch.all((dz.double().flatten() - n * slope).abs() <= 2.0 ** -6 * n.abs() + 1e-30)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,D", [(300, 21, 512), (70, 300, 128), (3, 1030, 64), (40, 5, 1024)])
+def test_many_heads(dtype, T, H, D):
+    """A block of tokens on several workgroups, the last of them with few heads."""
+    import gated_delta_rule_71_amd as gdr
+    from gated_delta_rule_71_amd import workloads as W
+    from test_gpu_group_norm import bounds, close, make
+    x, z, dy, w, b = make(9, T, H, D, dtype)
+    got = gdr.group_norm_backward(*(to_dev(a) for a in (x, w, dy, b)), z=to_dev(z))
+    xf, zf, df = W.as_f64(x), W.as_f64(z), W.as_f64(dy)
+    ref = GN.group_norm_backward(xf, w, df, b, zf)
+    tol = bounds(xf, zf, df, w.astype(float), b.astype(float), 1e-5, True)
+    for name, y, r in zip(("dx", "dw", "db", "dz"), got, ref):
+        close(y, r, tol[name], dtype == "bf16" and name in ("dx", "dz"), name)
