@@ -8,7 +8,8 @@
 // Streams bound by memory traffic: a row sits in the registers of LPR lanes, eight
 // channels and 16-byte accesses each, so the mean and the centred sum of squares are two
 // passes over registers, not over memory.  36112 tokens of 32 heads of 128, gated, bf16:
-// 888 MB in 170 us, 5.2 TB/s, what a large copy reaches; 24 tokens 3.0 us.
+// 888 MB in 173 us, 5.1 TB/s, what a large copy reaches; 24 tokens 3.3 us, of 8.1 us that
+// the host takes to call it.
 
 #include "common.hpp"
 #include "gdr_internal.hpp"
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(256) group_norm_kernel(const GroupNormParams p
 // gradient of its channels in registers over the tokens, the block adds its tl token
 // lanes through LDS and writes one row of partial sums, and a second kernel adds the
 // blocks' rows in a fixed order.  16384 tokens of 16 heads of 128, gated, bf16: 336 MB in
-// 70.5 us, 4.8 TB/s, and 4.6 us for the sums (1024 rows of 16 KB).
+// 80.4 us a call, 4.2 TB/s; 77 us traced, and 5.4 us for the sums (1024 rows of 16 KB).
 template <typename T, int LPR, int VPL, bool GATE>
 __global__ void __launch_bounds__(256) group_norm_backward_kernel(const GroupNormParams p) {
   constexpr int RPB = 256 / LPR, STEP = 8 * LPR;
@@ -332,7 +333,7 @@ int group_norm_backward_blocks(long tokens, int heads, int group) {
   // One workgroup per compute unit while the tokens last, up to four once each lane still
   // has eight tokens: more would write more partial sums than they hide latency (16384
   // tokens of 16 x 128 bf16 with a gate: 512 workgroups without prefetch 129 us, 1024
-  // with it 75 us; 1501 tokens of 5 x 96 float32: 62 workgroups 16.8 us, 256 10.4 us).
+  // with it 80 us; 1501 tokens of 5 x 96 float32: 62 workgroups 16.8 us, 256 10.4 us).
   int lpr = 4;
   while (lpr < 64 && 8 * lpr < group) lpr *= 2;
   const int rows = 256 / lpr, hb = heads < rows ? heads : rows;

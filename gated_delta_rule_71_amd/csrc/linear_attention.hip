@@ -17,9 +17,10 @@
 // where the reversed roles carry G, which is already decayed when the next token reads
 // it (off = 0), and put the scale into the state (s_intra = s_upd = scale, s_inter = 1).
 //
-// One workgroup runs one value head of a stretch of tokens through its chunks.  Each of
-// its DV/16 waves owns 16 value columns of the state, in accumulator registers for the
-// whole stretch; only the 64 x 64 (float32: 32 x 32) decayed scores pass between waves.
+// One workgroup runs one value head of a stretch of tokens through its chunks.  Each of its
+// waves (four; eight for sums at borders with DV = 128) owns DV/4 or DV/8 value columns of the
+// state, in accumulator registers for the whole stretch; only the 64 x 64 (float32: 32 x 32)
+// decayed scores pass between waves.
 //
 // Windows.  Without a delta rule a stretch's effect on the state is a decay and a sum, so
 // the packed tokens are cut at every `window` tokens, whatever the sequences, to fill the
@@ -30,15 +31,15 @@
 // border.  Only (1) and (3) read tokens, k and v twice and the rest once.
 //
 // Bounds (36112 packed tokens, 32 heads of 128 x 128 on 16 q/k heads, bf16: 0.92 GB that a
-// call must move, 182 us at a large copy's 5.07 TB/s; 344 us in all).  (3) takes 245 us:
-// 3.8 TB/s, with the matrix cores 25 percent and LDS 35 percent busy.  A chunk is a chain of
-// loads, LDS, products and barriers that two workgroups per compute unit (registers, LDS)
-// only partly hide: alone on its compute unit it takes as long as with a second one beside
-// it, and without its loads the pass would still take 0.87 of the time.  (1) takes 113 us
-// for k and v, (2) 7 us.
-// One long prompt (16383 tokens, 16 heads): 67, 38 and 12 us.  Gradients (4 x 4096 tokens,
-// 16 heads): 183 us for the three roles, which share operands in L2, 61 and 8 us.  Small
-// calls pay the start of a workgroup (6 of 13 us for 97 tokens: cold code, tables, states).
+// call must move, 182 us at a large copy's 5.07 TB/s; a call takes 422 us).  Medians of 200
+// traced calls: (3) 299 us, 3.1 TB/s, with the matrix cores 29 percent and LDS 30 percent
+// busy.  A chunk is a chain of loads, LDS, products and barriers that two workgroups per
+// compute unit (registers, LDS) only partly hide.  (1) takes 121 us for k and v, (2) 7 us.
+// One long prompt (16383 tokens, 16 heads, 129 us): 81, 42 and 12 us.  Gradients (4 x 4096
+// tokens, 16 heads, 268 us): 199 us for the three roles, which share operands in L2, 64 and
+// 8 us.  These have memories of one to 256 tokens; where all heads keep thousands, every token
+// is in reach of a border: 451, 138 and 275 us.  Small calls pay the start of a workgroup (6 of
+// 14 us for 97 tokens: cold code, tables, states).
 
 #include "common.hpp"
 #include "gdr_internal.hpp"
@@ -61,11 +62,12 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 //  * The state and the scores take two where they meet q and v.  A result that is rounded to
 //    bf16 then errs like the rounded exact one, and a float32 result keeps 16 bits of a term.
 //    With one part the outputs err by 0.0023 of their norm in place of 0.0017, float32 ones
-//    by as much (packed prefill 350 us in place of 405, gradients 246 in place of 264).
+//    by as much (packed prefill 366 us in place of 422, gradients 251 in place of 269).
 //  * The decayed values, which build the float32 states, take three where they are a part
 //    of a state that is handed out, so that it is as exact as a float32 sum: all tokens whose
 //    weight in it is not zero, as far ones can be all that it has (large at a prompt's start,
-//    zeros behind).  Two where the state only meets q.
+//    zeros behind; with two parts throughout 375 and 255 us).  Two where the state only
+//    meets q.
 // Matrix-core products a 64-token chunk at K = V = 128: 776 and 648 of 16x16x32; at a border
 // 384 and 256.
 
@@ -590,7 +592,9 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
               d[m] = O::mma(O::rows(lds.k, L::ldk, 16 * tj[m] + c, 32 * s, g),
                             O::rows(lds.q, L::ldq, 16 * ti[m] + c, 32 * s, g), d[m]);
         // A value that is not finite, times the zero scores of the tokens before it, would
-        // make those tokens' outputs NaN: up to such a token the chunks have one token.
+        // make those tokens' outputs NaN: up to such a token the chunks have one token.  Each
+        // of them is tried whole again first, which such inputs may cost: one NaN in the middle
+        // of 16383 tokens makes the call 507 us in place of 129, NaN throughout 4.6 ms.
         if (lds.mark) {
           __syncthreads();
           lds.mark = 0;
@@ -744,7 +748,7 @@ __global__ void __launch_bounds__(threads(DV, OUTPUT), OUTPUT ? 2 : 4) linear_at
 
 // The states at the borders from the windows' sums, four elements per thread, in place.
 // The chain along the borders is a multiply-add each; the loads of 16 borders are in flight
-// together (15 borders of 32 heads, 64 KB each: 7.2 us; eight at a time in
+// together (15 borders of 32 heads, 64 KB each: 7.3 us; eight at a time in
 // workgroups of four waves 10.5 us).
 constexpr int kCombineThreads = 64;
 __global__ void __launch_bounds__(kCombineThreads)
@@ -813,8 +817,9 @@ __global__ void __launch_bounds__(256)
 // One workgroup per (request, value head); thread t owns four value columns in every
 // (256 / (V/4))-th key row, so the state sits in registers between its read and its write,
 // which are all the traffic.  S' = lambda S + k v^T, then o = scale q S'.
-// 128 requests (112 live) of 32 heads of 128 x 128: 475 MB in 83 us, 5.7 TB/s; one request
-// 4.6 us, the trip to memory and back, of 10.5 us that the host takes to call it.
+// 128 requests (112 live) of 32 heads of 128 x 128: 475 MB in 97 us, 4.9 TB/s, what a large
+// copy reaches; one request 4.8 us, the trip to memory and back, of 10.7 us that the host
+// takes to call it.
 template <typename T, typename TOut, int DK, int DV>
 __global__ void __launch_bounds__(256) linear_decode_kernel(const LinearDecodeParams p) {
   constexpr int CG = DV / 4, RG = 256 / CG, RPT = DK / RG;
@@ -880,8 +885,8 @@ hipError_t launch_dims(LinearParams p, int dq, int dv, hipStream_t s) {
   const long places = linear_places(p, OUTPUT);
   // A head's 128 value columns go to two workgroups where one each would not give every
   // compute unit two: half the products per chunk for one more pass over q and k (2 x 1023
-  // tokens of 4 heads in float32, 128 workgroups: 37.0 us whole, 30.7 halved; 240 tokens of
-  // 64 heads in bf16, 64: 24.6 and 19.9; 16383 tokens of 16 heads in bf16, 512: 129 and 150).
+  // tokens of 4 heads in float32, 128 workgroups: 36.0 us whole, 29.0 halved; 240 tokens of
+  // 64 heads in bf16, 64: 28.8 and 22.5; 16383 tokens of 16 heads in bf16, 512: 129 and 149).
   p.halves = dv == 128 && places * p.H * p.roles <= 256;
   if (p.halves) dv = 64;
   const long sets = (places * p.Hk + 7) / 8 * 8;   // whole rounds over the XCDs
@@ -932,10 +937,10 @@ hipError_t launch_linear_borders(const LinearParams &p, int in_f32, int dq, int 
 }
 
 int linear_window(long tokens, int heads, int num_seqs, int packed, int roles) {
-  // Workgroups wanted: two per compute unit and role; with the three roles of the
-  // backward, three (packed prefill of 36112 tokens, 32 heads: 256 places 453 us, 512
-  // 368, 1024 395; one prompt of 16383 tokens, 16 heads: 122, 119, 146; backward of 4 x
-  // 4096 tokens, 16 heads: 248, 253, 304; calls in turn, clocks not at their best).
+  // Workgroups wanted: two per compute unit, as many as are resident; the three roles of the
+  // backward have 256 each, one round and a half (packed prefill of 36112 tokens, 32 heads: 256
+  // places 512 us, 512 422, 1024 440; one prompt of 16383 tokens, 16 heads: 137, 129, 154;
+  // backward of 4 x 4096 tokens, 16 heads: 128 places 311, 256 270, 512 282).
   const long places = roles > 1 ? 256 : 512;
   if (tokens <= 256 || (!packed && static_cast<long>(num_seqs) * heads >= places)) return 0;
   const long windows = (places + heads - 1) / heads;
