@@ -377,10 +377,11 @@ typedef struct {
  * structure or function before them.
  *
  * Arithmetic: float32 states, scores and sums for both input types.  With BF16 inputs the
- * state and the scores keep 16 bits where they meet q and v (float32 outputs too), and the
- * terms of the float32 states keep 24 bits; no value range narrower than bf16's applies.  A head's
- * weight lambda^n that is zero in float32 ends the reach of a token.  Inputs that are not
- * finite make the outputs of their own token and of later tokens of the sequence (in the
+ * state and the scores keep 16 bits where they meet q and v (float32 outputs too); the terms
+ * of the states keep 24 bits where a state is handed out and 16 where it stays inside, down
+ * to bf16's least spacing of 2^-133, and no value range narrower than bf16's applies.  A
+ * head's weight lambda^n that is zero in float32 ends the reach of a token.  Inputs that are
+ * not finite make the outputs of their own token and of later tokens of the sequence (in the
  * backward also of earlier ones) not finite; tokens out of their reach may be spared, and
  * which of NaN and infinity is not specified.  No other token, sequence or head is touched.
  *
